@@ -156,6 +156,8 @@ def _p(t):
         return None
     if not t.is_contiguous():
         raise ValueError("tensors passed to the SSD library must be contiguous")
+    if not t.is_cuda and not t.is_pinned():  # (a kernel reads pinned host memory, other host memory faults it)
+        raise ValueError("tensors passed to the SSD library must be on a GPU")
     return t.data_ptr()  # (argtypes says that it is a pointer)
 
 
