@@ -448,6 +448,8 @@ def _run(call, stream, tensors):
     call allocates belongs to that stream, its inputs are not reused before the stream is done with
     them, and its outputs are handed back to the caller's stream."""
     t = tensors[0]
+    if stream is not None and t.is_cuda and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
     if not t.is_cuda or (stream is None and t.device.index == torch.cuda.current_device()):
         return call()
     with torch.cuda.device(t.device):

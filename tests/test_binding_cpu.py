@@ -29,3 +29,11 @@ def test_tensors_of_the_host_are_refused():
                  lambda: ssd.backward(*ssd_in, ssd_in[0], chunk=64, stream=stream)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_a_stream_of_another_device_is_refused():
+    """A stand-in for a tensor of the first GPU, and a stream of the second one."""
+    t = types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", 0))
+    stream = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        ssd._run(lambda: pytest.fail("called"), stream, (t,))
