@@ -682,13 +682,9 @@ template <typename F> hipError_t by_dstate(int S, F&& f) {
     }
     return hipErrorInvalidValue;
 }
-// Computing waves a workgroup, each with 16 rows of the state: four, or fewer where the workgroups
-// still find a compute unit each. The waves of a workgroup read the same tiles from LDS, which holds
-// four of them up.
-template <typename F> hipError_t by_waves(const Dims& d, F&& f) {
-    const long slices = (long)d.batch * d.nheads * (d.headdim / 16);
-    int nw = std::min(4, d.headdim / 16);
-    while (nw > 1 && slices / (nw / 2) <= 256) nw /= 2;
+// f(the waves that walk `rows` rows of each of `heads` heads and segments)
+template <typename F> hipError_t by_waves(long heads, int rows, F&& f) {
+    const int nw = delta_waves(heads, rows);
     if (nw == 1) return f(std::integral_constant<int, 1>{});
     if (nw == 2) return f(std::integral_constant<int, 2>{});
     return f(std::integral_constant<int, 4>{});
@@ -697,14 +693,11 @@ template <typename F> hipError_t by_waves(const Dims& d, F&& f) {
 // nseg segments (1: none) of seg_chunks chunks; with segments, what comes before the walk for y.
 template <typename T, typename TO, int KIND>
 hipError_t walk(const DeltaArgs& a, const Dims& d, const DeltaSegs& sg, hipStream_t stream) {
-    const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC;
-    Dims wide = d;  // as many heads as there are segments to find units for
-    wide.nheads *= KIND == kDeltaSegment ? sg.nseg - 1 : sg.nseg;
-    wide.headdim = KIND == kDeltaSegment ? std::min(d.headdim, d.dstate) : d.headdim;
+    const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC, segs = KIND == kDeltaSegment ? sg.nseg - 1 : sg.nseg;
+    const int least = KIND == kDeltaSegment ? std::min(d.headdim, d.dstate) : d.headdim;  // a workgroup's rows divide it
     return by_dstate(d.dstate, [&](auto s) {
-        return by_waves(wide, [&](auto nw) {
+        return by_waves((long)d.batch * d.nheads * segs, least, [&](auto nw) {
             constexpr int NW = decltype(nw)::value;
-            const int segs = KIND == kDeltaSegment ? sg.nseg - 1 : sg.nseg;
             const int rows = KIND == kDeltaSegment ? d.headdim + d.dstate : d.headdim;
             const unsigned blocks = (unsigned)((long)d.batch * d.nheads * segs * (rows / (16 * NW)));
             delta_walk_kernel<T, decltype(s)::value, NW, TO, KIND><<<dim3(blocks), 64 * (NW + kDeltaLoaders), 0, stream>>>(
@@ -735,7 +728,7 @@ hipError_t walk_out(const DeltaArgs& a, const Dims& d, hipStream_t stream) {
 template <typename T> hipError_t reverse(const DeltaArgs& a, const Dims& d, hipStream_t stream) {
     const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC;
     return by_dstate(d.dstate, [&](auto s) {
-        return by_waves(d, [&](auto nw) {
+        return by_waves((long)d.batch * d.nheads, d.headdim, [&](auto nw) {
             constexpr int NW = decltype(nw)::value;
             const unsigned blocks = (unsigned)((long)d.batch * d.nheads * (d.headdim / (16 * NW)));
             delta_reverse_kernel<T, decltype(s)::value, NW><<<dim3(blocks), 64 * (NW + kDeltaLoaders), 0, stream>>>(

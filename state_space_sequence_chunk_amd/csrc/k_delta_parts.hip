@@ -21,24 +21,42 @@ __global__ __launch_bounds__(256) void delta_parts_kernel(const float* __restric
     *(f32x4*)(dq + at * 4) = y;
 }
 
+// Computing waves of a walk's workgroup, each with 16 rows of the state: four, or fewer where the workgroups
+// still find a compute unit each. The waves of a workgroup read the same tiles from LDS, which holds
+// four of them up.
+int delta_waves(long heads, int rows) {
+    const long slices = heads * (rows / 16);
+    int nw = std::min(4, rows / 16);
+    while (nw > 1 && slices / (nw / 2) <= 256) nw /= 2;
+    return nw;
+}
+
 // Segments cost a first walk of P + S rows instead of none and a carry, and let the walk for y run side by
-// side. The times are those measured at P 64, S 128 in bf16, in microseconds: 2.4 a chunk for a round of
-// 256 workgroups that walk 64 rows for y, 2.6 for one of 512 in the first walk, 3 a segment for the carry;
-// 65536 tokens of 8 heads took 456 us in one and 255 in 7 segments. In fp32 a chunk takes 2.6 times as long, and
-// one workgroup's tiles fill LDS (4096 tokens of 24 heads, P = S = 64: 162 us in one, 128 in 4).
+// side. Both plans are timed by the workgroups that the walks launch: 256 are walked at once (a second one on
+// a compute unit takes about as long again), a chunk after another. The times of a chunk, in microseconds, are
+// lines through those measured at dstate 16 to 256, headdim 16, 64 and 128, 2 to 96 heads, 2048 to 16384 tokens,
+// both types and every count of segments (6% off on average, the calls' times and prep's included). At those 810
+// shapes the plan taken is 2% slower on average than the best one (24% at worst) and takes 0.61 of one
+// segment's time (1.09 at worst). 65536 tokens of 8 heads 64 x 128, bf16: 496 us in one and 307 in 7 segments;
+// 16384 tokens of 48 heads 16 x 256: 924 us in one and 1076 in 3 segments.
 DeltaSegs delta_segments(int in_dtype, const Dims& d) {
+    const bool narrow = in_dtype == kBF16;
     const long nC = (d.seqlen + kDeltaC - 1) / kDeltaC, heads = (long)d.batch * d.nheads;
-    const long wide = heads * ((d.headdim + 63) / 64), unit = heads * ((d.dstate + 63) / 64);
-    auto rounds = [](long n, long at_once) { return (double)((n + at_once - 1) / at_once); };
+    const int P = d.headdim, S = d.dstate, least_rows = std::min(P, S);
+    const double first = narrow ? 0.42 + 0.005 * S : 1.4 + 0.02 * S, out = narrow ? 0.94 + 0.007 * S : 1.85 + 0.049 * S;
+    // microseconds a chunk for `rows` rows in all, nw waves a workgroup
+    auto chunk_time = [&](double one, long rows, int nw) {
+        const long wgs = rows / (16 * nw);
+        return one * (1 + (narrow ? 0.11 : 0.04) * (nw - 1)) * ((wgs + 255) / 256 + (narrow ? 0.0013 : 0.002) * S * wgs / 256);
+    };
     DeltaSegs best = {1, kDeltaNoSegments};
-    const double per = in_dtype == kBF16 ? 1.0 : 2.6;
-    const long at_once = in_dtype == kBF16 ? 512 : 256;
-    double least = per * nC * 1.9 * rounds(wide, 256);
+    double least = 0.93 * nC * chunk_time(out, heads * P, delta_waves(heads, P));
     for (long n = 3; n <= 16 && n * 8 <= nC; ++n) {
         const long chunks = (nC + n - 1) / n, nseg = (nC + chunks - 1) / chunks;
-        const double t = per * chunks * (2.6 * rounds((nseg - 1) * wide + (nseg - 2) * unit, at_once) + 2.4 * rounds(nseg * wide, 256)) +
-                         3.0 * nseg + 10;
-        if (t < 0.9 * least) {
+        const double t = chunks * (chunk_time(first, heads * ((nseg - 1) * P + (nseg - 2) * S), delta_waves(heads * (nseg - 1), least_rows)) +
+                                   chunk_time(out, heads * nseg * P, delta_waves(heads * nseg, P))) +
+                         6 + 0.02 * S * nseg;
+        if (t < least) {
             least = t;
             best = {(int)nseg, (int)chunks};
         }

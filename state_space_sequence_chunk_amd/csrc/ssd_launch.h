@@ -154,6 +154,8 @@ struct DeltaSegs {
 };
 constexpr int kDeltaNoSegments = 1 << 30;  // chunks of the one segment
 DeltaSegs delta_segments(int in_dtype, const Dims& d);
+// Computing waves of a walk's workgroup, for `rows` rows of each of `heads` heads (all batch rows and segments).
+int delta_waves(long heads, int rows);
 // Heads of a group are summed by this many workgroups a chunk in the backward pass.
 int delta_bwd_parts(const Dims& d);
 // One token at a time, the state in registers; final_state may be h0 itself.

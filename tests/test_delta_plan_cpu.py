@@ -1,0 +1,37 @@
+"""Plans of the gated delta rule's kernels, from the library's host-only queries (no GPU needed)."""
+import os
+
+import pytest
+
+from state_space_sequence_chunk_amd import ssd
+
+pytestmark = pytest.mark.skipif(not os.path.exists(ssd.LIB_PATH), reason="HIP library not built")
+
+
+def shape(batch, seqlen, nheads, headdim, dstate, ngroups=1, dtype=ssd.SSD_BF16):
+    return ssd.make_shape(batch, seqlen, nheads, headdim, dstate, ngroups, 64, dtype, ssd.SSD_F32)
+
+
+def segments(s):
+    """The forward walk's segments, from what its workspace holds beside each chunk's scalars and two
+    matrices: the states entering all segments, and the first walk's rows for all but the last."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    heads, P, S = s.batch * s.nheads, s.headdim, s.dstate
+    chunks = heads * (-(-s.seqlen // 64))
+    extra = ssd.delta_forward_workspace_bytes(s) - up(chunks * 5 * 64 * 4) - 2 * up(chunks * 6 * 2048)
+    fits = [n for n in range(2, 17) if up(4 * heads * (n - 1) * (P + S) * S) + up(4 * heads * n * P * S) == extra]
+    return fits[0] if extra else 1
+
+
+@pytest.mark.parametrize("nheads,headdim,dstate,most", [(32, 16, 256, 1), (48, 16, 256, 1), (48, 16, 128, 3), (96, 16, 256, 1)])
+def test_few_segments_where_the_first_walk_costs_more_than_it_saves(nheads, headdim, dstate, most):
+    # a first walk carries headdim + dstate rows; five segments of 32 and 48 heads of 16 x 256 measured 1.25 and
+    # 1.46 times one walk's time; 48 heads of 16 x 128: 1.16 in five segments, 0.93 in three
+    assert segments(shape(1, 16384, nheads, headdim, dstate)) <= most
+
+
+@pytest.mark.parametrize("s", [shape(4, 16384, 8, 64, 128), shape(1, 16384, 4, 16, 32), shape(1, 16384, 16, 128, 128),
+                               shape(1, 16384, 16, 64, 256, dtype=ssd.SSD_F32), shape(2, 2048, 24, 64, 64, dtype=ssd.SSD_F32)])
+def test_segments_where_they_pay(s):
+    # 0.2 to 0.8 times one walk's time
+    assert segments(s) > 1
