@@ -120,13 +120,13 @@ __device__ __forceinline__ Frag<T> row_frag_in(const T* base, size_t ld, int row
 }
 // Fragment of a column: slots kmap(g, v) are rows r0 + kmap(g, v), of which those at or past
 // `valid` are zero.
-template <int N, typename T>
+template <typename T>
 __device__ __forceinline__ Frag<T> col_frag_in(const T* col, size_t ld, int r0, int valid, int g) {
     Frag<T> f;
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
         const int r = r0 + 4 * g + (v & 3) + 16 * (v >> 2);
-        const bool in = r < valid && (v < 4 || N > 16);
+        const bool in = r < valid;
         const T x = col[(size_t)(in ? r : 0) * ld];
         f.v[v] = in ? x : (T)0.f;
     }
@@ -136,8 +136,6 @@ __device__ __forceinline__ Frag<T> col_frag_in(const T* col, size_t ld, int r0, 
 // 32-column tiles that hold a value: two planes of 64 lanes x 16 bytes a tile (bf16: high
 // parts, remainders; fp32: slots 0-3, slots 4-7). Lower tiles are (0,0) (1,0) (2,0) (2,1)
 // (3,0) (3,1); upper ones (transposes) (0,0) (0,1) (1,0) (1,1) (2,1) (3,1).
-constexpr int kDeltaTiles = 6;
-constexpr size_t kDeltaTileBytes = 2048, kDeltaMatBytes = kDeltaTiles * kDeltaTileBytes;
 __host__ __device__ constexpr int lower_tile(int ti, int kk) { return ti < 2 ? ti : 2 * ti - 2 + kk; }
 __host__ __device__ constexpr int upper_tile(int ti, int kk) { return ti < 2 ? 2 * ti + kk : ti + 2; }
 

@@ -67,8 +67,6 @@ Dims dims_of(const ssd_shape* s) {
     return d;
 }
 
-constexpr size_t kMat = 6 * 2048;  // bytes of one chunk's stored triangular matrix
-
 struct Sizes {
     size_t scal, mat, state, rows, part, ends, starts, total;
 };
@@ -78,7 +76,7 @@ Sizes sizes(const ssd_shape* s, bool backward) {
     if (d.seqlen == 0 || (!backward && ssd::delta_recurrent_preferred(s->in_dtype, d))) return z;
     const size_t n = (size_t)d.batch * d.nheads * d.nchunks();
     z.scal = round_up(n * ssd::kDeltaScal * sizeof(float));
-    z.mat = round_up(n * kMat);
+    z.mat = round_up(n * ssd::kDeltaMatBytes);
     z.total = z.scal + 2 * z.mat;
     if (!backward) {
         const ssd::DeltaSegs sg = ssd::delta_segments(s->in_dtype, d);

@@ -139,10 +139,10 @@ template <typename T, int S, int P> struct GradsCfg {
 template <typename T, int S, int P>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(GradsCfg<T, S, P>::PAIR ? 2 : 1, 2))) void delta_grads_kernel(
     const T* __restrict__ k, const T* __restrict__ q, const T* __restrict__ v,
-    const float* __restrict__ gl, const float* __restrict__ scal, const char* __restrict__ Hc,
-    const char* __restrict__ Ec, const char* __restrict__ Ut, const char* __restrict__ Nt,
-    const char* __restrict__ Zt, float* __restrict__ dg, float* __restrict__ dbeta,
-    float* __restrict__ dk, float* __restrict__ dq, int L, int H, int ngroups, int nC, int parts) {
+    const float* __restrict__ scal, const char* __restrict__ Hc, const char* __restrict__ Ec,
+    const char* __restrict__ Ut, const char* __restrict__ Nt, const char* __restrict__ Zt,
+    float* __restrict__ dg, float* __restrict__ dbeta, float* __restrict__ dk, float* __restrict__ dq,
+    int L, int H, int ngroups, int nC, int parts) {
     using Cfg = GradsCfg<T, S, P>;
     using ST = typename Cfg::ST;
     using TT = typename Cfg::TT;
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(GradsCfg<T,
         };
         auto cols_of = [&](int m, int t, int x) {
             if constexpr (Cfg::KQ) return ad.plain_cols(kq + m * Cfg::KB, t, x);
-            else return col_frag_in<32>((m ? qc : kc) + 16 * t + here(c), ld, 32 * x, valid, g);
+            else return col_frag_in((m ? qc : kc) + 16 * t + here(c), ld, 32 * x, valid, g);
         };
         auto acc_of = [&](int m, int t) {  // this wave's rows, as an accumulator holds them
             if constexpr (Cfg::KQ) {
@@ -549,7 +549,7 @@ template <typename T, int S> hipError_t delta_grads(const DeltaArgs& a, const Di
     const unsigned blocks = (unsigned)((long)d.batch * nC * d.ngroups * parts);
     auto go = [&](auto p) {
         delta_grads_kernel<T, S, decltype(p)::value><<<dim3(blocks), 256, 0, stream>>>(
-            (const T*)a.k, (const T*)a.q, (const T*)a.v, a.g, a.scal, a.Hc, a.Ec, a.Ut, a.Nt, a.Zt, a.dg, a.dbeta,
+            (const T*)a.k, (const T*)a.q, (const T*)a.v, a.scal, a.Hc, a.Ec, a.Ut, a.Nt, a.Zt, a.dg, a.dbeta,
             parts > 1 ? a.dkp : a.dk, parts > 1 ? a.dqp : a.dq, d.seqlen, d.nheads, d.ngroups, nC, parts);
         return hipGetLastError();
     };

@@ -128,7 +128,8 @@ hipError_t launch_chunk_out_seg(int out_dtype, const void* x, const void* Bm, co
 // buffer is the caller's. `scal` holds, per (batch, head, chunk), kDeltaChunk values each of
 // e^{G_i}, e^{G_C - G_i} and beta_i and, in the backward pass, G_i log2(e) in 64 bits (kDeltaScal
 // floats in all); the matrices are the tile stores of delta.h.
-constexpr int kDeltaChunk = 64, kDeltaScal = 5 * kDeltaChunk;
+constexpr int kDeltaChunk = 64, kDeltaScal = 5 * kDeltaChunk, kDeltaTiles = 6;
+constexpr size_t kDeltaTileBytes = 2048, kDeltaMatBytes = kDeltaTiles * kDeltaTileBytes;  // a stored triangular matrix
 struct DeltaArgs {
     const void *v, *beta, *k, *q;
     const float *g, *h0;
