@@ -363,6 +363,20 @@ ssd_status ssd_delta_backward(const ssd_shape* shape, const void* v, const float
                               void* stream);
 
 /*
+ * The plans of the delta rule's kernels for a shape (host-only). Any of the outputs may be NULL. All are
+ * 0 where no chunked kernel runs (seqlen 0; forward: also sequences that run token by token).
+ * segments: runs of chunks that the forward walk is cut into (1: one walk over all chunks);
+ * waves: computing waves of a workgroup of the walk for y (backward: of both walks), each with 16 rows
+ * of a state; first_waves: those of the first walk over the segments (0 without); prep_heads: heads of
+ * a group that one wave prepares one after another; grad_heads: the most heads of a group whose
+ * gradients one workgroup takes one after another.
+ */
+ssd_status ssd_delta_forward_plan(const ssd_shape* shape, int32_t* segments, int32_t* waves,
+                                  int32_t* first_waves, int32_t* prep_heads);
+ssd_status ssd_delta_backward_plan(const ssd_shape* shape, int32_t* waves, int32_t* prep_heads,
+                                   int32_t* grad_heads);
+
+/*
  * Group norm with an activation, channels last: the norm that closes a mixer layer. For each
  * token, the channels are cut into `groups` runs of n = channels / groups, each with its own
  * statistics (a token's output depends on that token alone, as a causal layer needs):

@@ -161,6 +161,26 @@ ssd_status ssd_delta_forward(const ssd_shape* shape, const void* v, const float*
     return status_of(e);
 }
 
+ssd_status ssd_delta_forward_plan(const ssd_shape* shape, int32_t* segments, int32_t* waves,
+                                  int32_t* first_waves, int32_t* prep_heads) {
+    const ssd_status st = check(shape, true);
+    if (st != SSD_OK) return st;
+    const Dims d = dims_of(shape);
+    int n = 0, w = 0, first = 0, hb = 0;
+    if (sizes(shape, false).total > 0) {
+        const long heads = (long)d.batch * d.nheads;
+        n = ssd::delta_segments(shape->in_dtype, d).nseg;
+        w = ssd::delta_waves(heads * n, d.headdim);
+        first = n > 1 ? ssd::delta_waves(heads * (n - 1), ssd::delta_first_rows(d)) : 0;
+        hb = ssd::delta_prep_heads(d);
+    }
+    if (segments) *segments = n;
+    if (waves) *waves = w;
+    if (first_waves) *first_waves = first;
+    if (prep_heads) *prep_heads = hb;
+    return SSD_OK;
+}
+
 ssd_status ssd_delta_decode_step(const ssd_shape* shape, const void* v, const float* g, const void* beta,
                                  const void* k, const void* q, const float* state, float scale,
                                  float* state_out, float* y, void* stream) {
@@ -180,6 +200,19 @@ ssd_status ssd_delta_backward_workspace_bytes(const ssd_shape* shape, size_t* by
     const ssd_status st = check(shape, false);
     if (st != SSD_OK) return st;
     *bytes = sizes(shape, true).total;
+    return SSD_OK;
+}
+
+ssd_status ssd_delta_backward_plan(const ssd_shape* shape, int32_t* waves, int32_t* prep_heads,
+                                   int32_t* grad_heads) {
+    const ssd_status st = check(shape, false);
+    if (st != SSD_OK) return st;
+    const Dims d = dims_of(shape);
+    const bool empty = d.seqlen == 0;
+    const int hpg = d.nheads / d.ngroups, parts = ssd::delta_bwd_parts(d);
+    if (waves) *waves = empty ? 0 : ssd::delta_waves((long)d.batch * d.nheads, d.headdim);
+    if (prep_heads) *prep_heads = empty ? 0 : ssd::delta_prep_heads(d);
+    if (grad_heads) *grad_heads = empty ? 0 : (hpg + parts - 1) / parts;
     return SSD_OK;
 }
 

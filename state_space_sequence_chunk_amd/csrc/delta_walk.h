@@ -694,7 +694,7 @@ template <typename F> hipError_t by_waves(long heads, int rows, F&& f) {
 template <typename T, typename TO, int KIND>
 hipError_t walk(const DeltaArgs& a, const Dims& d, const DeltaSegs& sg, hipStream_t stream) {
     const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC, segs = KIND == kDeltaSegment ? sg.nseg - 1 : sg.nseg;
-    const int least = KIND == kDeltaSegment ? std::min(d.headdim, d.dstate) : d.headdim;  // a workgroup's rows divide it
+    const int least = KIND == kDeltaSegment ? delta_first_rows(d) : d.headdim;
     return by_dstate(d.dstate, [&](auto s) {
         return by_waves((long)d.batch * d.nheads * segs, least, [&](auto nw) {
             constexpr int NW = decltype(nw)::value;

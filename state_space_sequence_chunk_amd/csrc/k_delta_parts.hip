@@ -42,7 +42,7 @@ int delta_waves(long heads, int rows) {
 DeltaSegs delta_segments(int in_dtype, const Dims& d) {
     const bool narrow = in_dtype == kBF16;
     const long nC = (d.seqlen + kDeltaC - 1) / kDeltaC, heads = (long)d.batch * d.nheads;
-    const int P = d.headdim, S = d.dstate, least_rows = std::min(P, S);
+    const int P = d.headdim, S = d.dstate;
     const double first = narrow ? 0.42 + 0.005 * S : 1.4 + 0.02 * S, out = narrow ? 0.94 + 0.007 * S : 1.85 + 0.049 * S;
     // microseconds a chunk for `rows` rows in all, nw waves a workgroup
     auto chunk_time = [&](double one, long rows, int nw) {
@@ -53,7 +53,7 @@ DeltaSegs delta_segments(int in_dtype, const Dims& d) {
     double least = 0.93 * nC * chunk_time(out, heads * P, delta_waves(heads, P));
     for (long n = 3; n <= 16 && n * 8 <= nC; ++n) {
         const long chunks = (nC + n - 1) / n, nseg = (nC + chunks - 1) / chunks;
-        const double t = chunks * (chunk_time(first, heads * ((nseg - 1) * P + (nseg - 2) * S), delta_waves(heads * (nseg - 1), least_rows)) +
+        const double t = chunks * (chunk_time(first, heads * ((nseg - 1) * P + (nseg - 2) * S), delta_waves(heads * (nseg - 1), delta_first_rows(d))) +
                                    chunk_time(out, heads * nseg * P, delta_waves(heads * nseg, P))) +
                          6 + 0.02 * S * nseg;
         if (t < least) {
@@ -62,6 +62,15 @@ DeltaSegs delta_segments(int in_dtype, const Dims& d) {
         }
     }
     return best;
+}
+
+// The largest divisor of the group's heads that leaves two rounds of eight waves a compute unit.
+int delta_prep_heads(const Dims& d) {
+    const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC, hpg = d.nheads / d.ngroups;
+    int hb = 1;
+    for (int n = 1; n <= hpg; ++n)
+        if (hpg % n == 0 && (long)d.batch * nC * d.ngroups * (hpg / n) >= 4096) hb = n;
+    return hb;
 }
 
 // As many parts as give four workgroups a compute unit, at most one for every head.

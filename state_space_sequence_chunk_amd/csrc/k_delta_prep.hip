@@ -233,12 +233,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
 template <typename T, bool BWD>
 static hipError_t prep_by_s(const DeltaArgs& a, const Dims& d, hipStream_t stream) {
-    const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC, hpg = d.nheads / d.ngroups;
-    // heads of a group a wave takes one after another: the largest divisor that leaves two rounds
-    // of eight waves a compute unit
-    int hb = 1;
-    for (int n = 1; n <= hpg; ++n)
-        if (hpg % n == 0 && (long)d.batch * nC * d.ngroups * (hpg / n) >= 4096) hb = n;
+    const int nC = (d.seqlen + kDeltaC - 1) / kDeltaC, hpg = d.nheads / d.ngroups, hb = delta_prep_heads(d);
     const long tasks = (long)d.batch * nC * d.ngroups * (hpg / hb);
     auto go = [&](auto s) {
         delta_prep_kernel<T, decltype(s)::value, BWD><<<dim3((unsigned)((tasks + 3) / 4)), 256, 0, stream>>>(

@@ -157,6 +157,10 @@ constexpr int kDeltaNoSegments = 1 << 30;  // chunks of the one segment
 DeltaSegs delta_segments(int in_dtype, const Dims& d);
 // Computing waves of a walk's workgroup, for `rows` rows of each of `heads` heads (all batch rows and segments).
 int delta_waves(long heads, int rows);
+// Rows of the state whose count the first walk's workgroups divide into (they hold rows of both kinds).
+inline int delta_first_rows(const Dims& d) { return d.headdim < d.dstate ? d.headdim : d.dstate; }
+// Heads of a group that a wave prepares one after another.
+int delta_prep_heads(const Dims& d);
 // Heads of a group are summed by this many workgroups a chunk in the backward pass.
 int delta_bwd_parts(const Dims& d);
 // One token at a time, the state in registers; final_state may be h0 itself.

@@ -30,6 +30,7 @@ EXPORTS = ("ssd_status_string", "ssd_validate_shape", "ssd_forward_workspace_byt
            "ssd_chunk_out_segmented", "ssd_segment_plan", "ssd_forward_noalloc",
            "ssd_chunk_out_plan", "ssd_delta_forward_workspace_bytes", "ssd_delta_forward",
            "ssd_delta_decode_step", "ssd_delta_backward_workspace_bytes", "ssd_delta_backward",
+           "ssd_delta_forward_plan", "ssd_delta_backward_plan",
            "ssd_group_norm", "ssd_group_norm_backward_workspace_bytes", "ssd_group_norm_backward")
 # Activations of the group norm (ssd_act in ssd.h).
 ACTS = {"none": 0, "silu": 1, "gate_pre": 2, "gate_post": 3}
@@ -101,6 +102,8 @@ def load_library():
     lib.ssd_delta_decode_step.argtypes = [sp] + [vp] * 6 + [f32] + [vp] * 3
     lib.ssd_delta_backward_workspace_bytes.argtypes = [sp, ctypes.POINTER(sz)]
     lib.ssd_delta_backward.argtypes = [sp] + [vp] * 8 + [f32] + [vp] * 7 + [sz, vp]
+    lib.ssd_delta_forward_plan.argtypes = [sp] + [i32p] * 4
+    lib.ssd_delta_backward_plan.argtypes = [sp] + [i32p] * 3
     np_ = ctypes.POINTER(ssd_norm_shape)
     lib.ssd_group_norm.argtypes = [np_] + [vp] * 6
     lib.ssd_group_norm_backward_workspace_bytes.argtypes = [np_, ctypes.POINTER(sz)]
@@ -479,6 +482,22 @@ def delta_backward_workspace_bytes(shape: ssd_shape) -> int:
     _check(load_library().ssd_delta_backward_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)),
            "ssd_delta_backward_workspace_bytes")
     return int(n.value)
+
+
+def delta_forward_plan(shape: ssd_shape):
+    """(segments, waves a workgroup, waves a workgroup of the first walk over segments, heads a wave
+    prepares) of the delta rule's forward pass; zeros where no chunked kernel runs."""
+    n = [ctypes.c_int32(0) for _ in range(4)]
+    _check(load_library().ssd_delta_forward_plan(ctypes.byref(shape), *map(ctypes.byref, n)), "ssd_delta_forward_plan")
+    return tuple(int(x.value) for x in n)
+
+
+def delta_backward_plan(shape: ssd_shape):
+    """(waves a workgroup of the walks, heads a wave prepares, heads a workgroup takes the gradients of)
+    of the delta rule's backward pass; zeros for an empty sequence."""
+    n = [ctypes.c_int32(0) for _ in range(3)]
+    _check(load_library().ssd_delta_backward_plan(ctypes.byref(shape), *map(ctypes.byref, n)), "ssd_delta_backward_plan")
+    return tuple(int(x.value) for x in n)
 
 
 def ssd_delta_forward(shape, v, g, beta, k, q, h0, scale, y, final_state, workspace, stream=None):

@@ -1,4 +1,5 @@
 """Plans of the gated delta rule's kernels, from the library's host-only queries (no GPU needed)."""
+import ctypes
 import os
 
 import pytest
@@ -35,3 +36,25 @@ def test_few_segments_where_the_first_walk_costs_more_than_it_saves(nheads, head
 def test_segments_where_they_pay(s):
     # 0.2 to 0.8 times one walk's time
     assert segments(s) > 1
+
+
+def test_plans():
+    # the 2.7B layer: four waves a workgroup, ten of the group's 80 heads prepared by a wave, 40 a workgroup's gradients
+    big = shape(2, 16384, 80, 64, 128)
+    assert ssd.delta_forward_plan(big) == (1, 4, 0, 10) and ssd.delta_backward_plan(big) == (4, 10, 40)
+    assert ssd.delta_backward_plan(shape(4, 4096, 48, 64, 128)) == (4, 3, 12)
+    # few rows: a workgroup each
+    assert ssd.delta_forward_plan(shape(1, 100, 2, 64, 64)) == (1, 1, 0, 1)
+    assert ssd.delta_backward_plan(shape(1, 100, 2, 64, 64)) == (1, 1, 1)
+    # no chunked kernel: token by token, or nothing
+    assert ssd.delta_forward_plan(shape(2, 16, 80, 64, 128)) == (0, 0, 0, 0)
+    assert ssd.delta_backward_plan(shape(2, 16, 80, 64, 128)) == (4, 1, 1)
+    assert ssd.delta_forward_plan(shape(2, 0, 8, 64, 128)) == (0, 0, 0, 0)
+    assert ssd.delta_backward_plan(shape(2, 0, 8, 64, 128)) == (0, 0, 0)
+    for s in (shape(4, 16384, 8, 64, 128), shape(1, 4099, 24, 64, 64)):
+        assert ssd.delta_forward_plan(s)[0] == segments(s) > 1
+    lib = ssd.load_library()
+    assert lib.ssd_delta_forward_plan(ctypes.byref(big), None, None, None, None) == 0
+    assert lib.ssd_delta_backward_plan(ctypes.byref(big), None, None, None) == 0
+    assert lib.ssd_delta_forward_plan(ctypes.byref(shape(2, 100, 8, 48, 128)), None, None, None, None) == 4
+    assert lib.ssd_delta_backward_plan(None, None, None, None) == 1
