@@ -133,7 +133,11 @@ template <typename T, int S, int P> struct GradsCfg {
     // K and Q are read from memory where they do not fit beside the region
     static constexpr bool KQ = 2 * KB + REGION + SMALL <= 163840;
     static constexpr int LDS = (KQ ? 2 * KB : 0) + REGION;
-    static constexpr bool PAIR = P <= 64 && 2 * (LDS + SMALL) <= 163840;  // two workgroups a compute unit
+    // Two workgroups a compute unit, each with half the registers, where K and Q are in LDS too. Where they are
+    // not (fp32, dstate 256) their fragments are formed from memory and half the registers would put 750 to 980
+    // values in scratch memory: the backward pass of 2 x 4096 tokens of 24 heads takes 3632 us so and 3088 with
+    // one workgroup at headdim 32, 3914 and 3333 at 64.
+    static constexpr bool PAIR = KQ && P <= 64 && 2 * (LDS + SMALL) <= 163840;
 };
 
 template <typename T, int S, int P>

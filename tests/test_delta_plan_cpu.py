@@ -1,6 +1,7 @@
 """Plans of the gated delta rule's kernels, from the library's host-only queries (no GPU needed)."""
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -58,3 +59,18 @@ def test_plans():
     assert lib.ssd_delta_backward_plan(ctypes.byref(big), None, None, None) == 0
     assert lib.ssd_delta_forward_plan(ctypes.byref(shape(2, 100, 8, 48, 128)), None, None, None, None) == 4
     assert lib.ssd_delta_backward_plan(None, None, None, None) == 1
+
+
+ASM = os.path.join(os.path.dirname(ssd.LIB_PATH), "..", "_build", "k_delta_grads_f32.hip.s")
+
+
+@pytest.mark.skipif(not os.path.exists(ASM), reason="no kernel assembly (written by the build)")
+@pytest.mark.parametrize("headdim", [32, 64])
+def test_gradients_at_dstate_256_take_all_registers(headdim):
+    # held to half of them these instances of the fp32 gradients' kernel kept more than 2100 bytes a lane in scratch
+    # memory and made the backward pass 15 to 25% slower
+    text = open(ASM).read()
+    name = f"delta_grads_kernelIfLi256ELi{headdim}EE"
+    entry = [k for k in text[text.index("amdhsa.kernels:"):].split("  - .agpr_count:")[1:] if name in k]
+    assert len(entry) == 1
+    assert int(re.search(r"\.private_segment_fixed_size: (\d+)", entry[0]).group(1)) < 1024
