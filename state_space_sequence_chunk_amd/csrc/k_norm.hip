@@ -328,10 +328,13 @@ NormRows norm_rows(const NormPlan& p, long tokens, int groups) {
         }
     }
     const long turns = (tokens + r.tpw - 1) / r.tpw;
-    // Two workgroups a compute unit (four: 300 us, two: 288 at 16384 x 5120), or four where each makes at most
-    // eight turns and the wait for a turn's sums counts (1001 x 1683 in 9 groups with the rows' sums: two 22.7
-    // us, four 20.5, eight 25.8).
-    const long want = std::max(1L, (turns * r.gblocks <= 8 * 512 ? 1024L : 512L) / r.gblocks);
+    // As many workgroups as the compute units hold at once, which the registers for a thread's channels decide: four
+    // with up to five channels a thread, three with twelve, two with more or with 1024 threads (eight channels: two
+    // and four take the same time). In us with 512, 768 and 1024 workgroups: 16000 x 1024 in one group (four channels)
+    // 88, 66, 59; 8000 x 1683 in 9 (three) 101, 71, 59; 16000 x 2700 in one (twelve) 195, 154, 201; 16000 x 2048 in one
+    // (eight) 118, 145, 118; 16384 x 5120 in 8 (twenty) 284, 361, 294.
+    const int held = p.vec * p.k;
+    const long want = std::max(1L, (p.threads > 256 ? 512L : held <= 5 ? 1024L : held == 12 ? 768L : 512L) / r.gblocks);
     r.tblocks = (int)std::max(1L, std::min(std::min(turns, want), std::max(1L, 2048L / r.tpw)));
     return r;
 }

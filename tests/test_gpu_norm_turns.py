@@ -24,7 +24,7 @@ SIZES = [
     (2100, 768, 1),    # 3 of 64; forwards, in vectors of 8, 3 of 32
     (9001, 64, 1),     # 1 of 16, many turns
     (1001, 1683, 9),   # single channels, 3 of 64
-    (2049, 516, 1),    # 1 of 256 with threads that hold none
+    (2049, 516, 1),    # 5 of 32, threads that hold no channel
     (33000, 48, 3),    # 1 of 4: 64 groups' threads a workgroup
 ]
 
