@@ -39,6 +39,16 @@ def test_segments_where_they_pay(s):
     assert segments(s) > 1
 
 
+@pytest.mark.parametrize("batch,seqlen,nheads,headdim,dstate,dtype,loop", [
+    (96, 16, 32, 128, 256, ssd.SSD_BF16, False), (96, 24, 32, 128, 256, ssd.SSD_F32, False), (32, 16, 32, 64, 128, ssd.SSD_BF16, False),
+    (96, 24, 32, 16, 16, ssd.SSD_BF16, True), (1, 32, 2, 128, 256, ssd.SSD_F32, True), (2, 16, 80, 64, 128, ssd.SSD_BF16, True),
+    (96, 1, 32, 128, 256, ssd.SSD_BF16, True), (1, 65, 1, 16, 16, ssd.SSD_F32, False)])
+def test_token_by_token_where_it_is_faster(batch, seqlen, nheads, headdim, dstate, dtype, loop):
+    # 948 us token by token and 353 by chunks (first), 1413 and 724, 77 and 38; 30 and 53, 22 and 47, 19 and 21
+    s = shape(batch, seqlen, nheads, headdim, dstate, dtype=dtype)
+    assert (ssd.delta_forward_workspace_bytes(s) == 0) == loop
+
+
 def test_plans():
     # the 2.7B layer: four waves a workgroup, ten of the group's 80 heads prepared by a wave, 40 a workgroup's gradients
     big = shape(2, 16384, 80, 64, 128)

@@ -31,7 +31,7 @@ CASES = [
     ((130, 65, 6, 64, 32, 1), (4, 1, 2)),    # four parts: 1, 2, 1 and 2 heads
     ((260, 65, 4, 128, 64, 2), (4, 1, 2)),
     ((280, 65, 4, 64, 256, 1), (4, 1, 2)),
-    ((1050, 40, 3, 16, 16, 1), (1, 1, 3)),
+    ((1050, 65, 3, 16, 16, 1), (1, 1, 3)),
     ((1050, 40, 3, 64, 128, 1), (4, 1, 3)),
     ((350, 130, 12, 32, 16, 1), (2, 3, 12)),
 ]
@@ -43,6 +43,16 @@ SEGMENTS = [
     ((1, 4099, 16, 128, 64, 1), (6, 4, 2)),
     ((1, 4099, 24, 64, 64, 1), (8, 4, 4)),
     ((1, 4099, 24, 128, 128, 8), (4, 4, 4)),
+]
+
+# whether the sequence runs token by token, in bf16 and fp32: by what both ways cost, up to 64 tokens
+SHORT = [
+    ((1, 33, 2, 16, 16, 1), (True, True)),
+    ((1, 48, 2, 64, 256, 1), (False, True)),
+    ((2, 64, 1, 16, 16, 1), (False, False)),
+    ((96, 16, 32, 64, 128, 4), (False, True)),
+    ((96, 7, 32, 16, 64, 2), (True, True)),
+    ((40, 5, 16, 128, 256, 1), (True, True)),
 ]
 
 
@@ -89,6 +99,17 @@ def test_backward(shape, plan, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape,loop", SHORT)
+def test_short_sequences(shape, loop, dtype):
+    e = _problem(shape, dtype, sum(shape))
+    assert (ssd.delta_forward_plan(_shape(e))[0] == 0) == loop[dtype == "fp32"]
+    y, final = ssd.delta_forward(*[e[n] for n in INPUTS], scale=0.5)
+    want_y, want_f, _ = ref.forward(e, 0.5)
+    _close(y, want_y, TOL[dtype], "y")
+    _close(final, want_f, TOL[dtype], "final")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("shape,plan", SEGMENTS)
 def test_forward_by_segments(shape, plan, dtype):
     e = _problem(shape, dtype, sum(shape), gmin=-0.02)  # a state that lasts from segment to segment
@@ -101,7 +122,7 @@ def test_forward_by_segments(shape, plan, dtype):
 
 def test_nan_in_one_head_of_many():
     # a workgroup's gradients go head by head: what a head leaves in LDS does not reach the next
-    shape = (1050, 40, 3, 16, 16, 1)
+    shape = (1050, 65, 3, 16, 16, 1)
     e = _problem(shape, "bf16", 9)
     assert ssd.delta_backward_plan(_shape(e))[2] == 3
     args = lambda: [e[n] for n in INPUTS] + [e["dy"], e["dfinal"]]  # noqa: E731
