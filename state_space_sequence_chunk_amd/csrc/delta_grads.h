@@ -16,8 +16,8 @@
 // at a time (everything is a sum over P). The bound is that traffic, 4 (2 S + 3 * 64) P bytes a head,
 // and the waits for it: a workgroup's next piece has no room while the last one is read, so that only the
 // other workgroup of the compute unit (two fit at dstate 128) keeps memory busy. 16384 tokens of 48 heads of
-// 64 x 128 in bf16: 1.4 GB in 463 to 520 us (2801 read from memory where used, 1300 through LDS, 724 with
-// loads beside products, 665 with products in groups of tiles, 509 without values held in scratch memory).
+// 64 x 128 in bf16: 1.4 GB in 433 to 504 us (2801 read from memory where used, 1300 through LDS, 724 with
+// loads beside products, 665 with products in groups of tiles, 509 with 16 bytes of a lane in scratch memory).
 #pragma once
 
 #include "delta_walk.h"

@@ -12,7 +12,8 @@
 // between them, 1.9 us at dstate 128 in bf16 (a workgroup of four such waves a compute unit, each on its
 // own SIMD). 32768 tokens of 80 heads of 64 x 128 in two sequences took 5819 us with rows and matrices read
 // from memory where they were used, 951 with them in LDS a chunk ahead, 791 with tiles read 16 bytes at a
-// time, 691 with a wave that only loads, and takes some 560 with four of them and the products interleaved.
+// time, 691 with a wave that only loads, and takes 576 with four of them and the products interleaved (665 in a
+// process's first calls).
 // What the backward pass keeps is bound by memory: at 16384 tokens of 48 heads in four sequences the walk
 // that stores H and U takes 193 us and the reverse walk 335 us, at about 4.4 TB/s.
 #pragma once

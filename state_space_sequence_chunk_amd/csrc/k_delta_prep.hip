@@ -17,7 +17,7 @@
 // stand. T^T in accumulators is T as the walk's operand.
 //
 // Bound by the matrices' way to memory, 24 KiB a head (backward 36): at 32768 tokens of 80 heads
-// 1.0 GB in 212 us, 4.8 TB/s (644 us with a workgroup a chunk, its waves waiting at barriers); backward at
+// 1.0 GB in 215 us, 4.8 TB/s (644 us with a workgroup a chunk, its waves waiting at barriers); backward at
 // 16384 tokens of 48 heads 0.47 GB in 100 to 108 us.
 #include <type_traits>
 

@@ -12,8 +12,8 @@
 // then a butterfly, then LDS where a group takes more than one wave. The mean is taken first
 // and the squares of the differences after it, from the registers.
 //
-// 32768 x 5120 bf16 channels with a gate, 1.0 GB: 182 us, 5.5 TB/s; two rows of 5120: 4.2 us; backwards
-// 16384 x 5120 with bf16 x and z, 1.3 GB: 278 us with its parameters, 4.8 TB/s.
+// 32768 x 5120 bf16 channels with a gate, 1.0 GB: 181 us, 5.6 TB/s; two rows of 5120: 4.2 us; backwards
+// 16384 x 5120 with bf16 x and z, 1.3 GB: 283 us with its parameters, 4.7 TB/s.
 //
 // Backwards a thread keeps its channels over all the tokens it takes and adds up dw and db
 // for them in registers; the rows of partial sums are added in a fixed order by a second

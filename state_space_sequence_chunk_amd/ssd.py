@@ -525,7 +525,8 @@ def ssd_delta_backward(shape, v, g, beta, k, q, h0, dy, dfinal, scale, dv, dg, d
 def delta_forward(v, g, beta, k, q, h0=None, *, scale=1.0, out_dtype=None, stream=None):
     """Gated delta rule over whole sequences: v [b, L, h, P], g (fp32 log decays) and beta
     [b, L, h], k and q [b, L, groups, S], optional state h0 (fp32 [b, h, P, S]). Returns
-    (y [b, L, h, P] in out_dtype (fp32 by default), final state fp32 [b, h, P, S])."""
+    (y [b, L, h, P] in out_dtype (fp32 by default), final state fp32 [b, h, P, S]). With bf16 inputs
+    products keep 16 bits of fp32 values; fp32 inputs keep all 24."""
     if v.dim() != 4:
         raise ValueError("v is [b, L, h, P]")
     _check_delta(v, g, beta, k, q, (("h0", h0),))
@@ -642,7 +643,8 @@ def _norm_shape_of(x, weight, bias, z, dy, groups, eps, center, act, out_dtype):
 
 def group_norm(x, weight=None, bias=None, *, z=None, groups=1, eps=1e-5, center=False, act="none",
                out_dtype=None, stream=None):
-    """Group norm of each token's channels with an activation: x [..., channels] (bf16 or fp32),
+    """Group norm of each token's channels with an activation. The statistics are each token's own, as a
+    causal layer needs (torch.nn.GroupNorm takes them over a sequence too). x [..., channels] (bf16 or fp32),
     act "none", "silu", "gate_pre" (norm of x * silu(z)) or "gate_post" (norm times silu(z)), the
     mean subtracted where center is true. weight and bias are fp32 [channels] or None. Returns the
     output in out_dtype (fp32 by default)."""
