@@ -119,9 +119,10 @@ hipError_t launch_delta_recurrent(int in_dtype, int out_dtype, const DeltaArgs& 
 
 // The loop's time is its steps', one behind the other: 0.5 us and 0.53 for a million elements of the states. A
 // chunk takes its launches and its way through both kernels whatever its tokens, and then its matrices and
-// states. Lines through calls of 8 to 48 tokens with 2 to 3072 states of 16 x 16 to 128 x 256, both types, through
+// states. Lines through calls of 8 to 48 tokens with 2 states to 96 sequences of 32 heads, 16 x 16 to 128 x 256, both types, through
 // the binding: the choice is 0.7% slower there than the better of both on average (33% at worst). 16 tokens in bf16
-// token by token and by chunks: 160 states of 64 x 128 19 and 21 us, 3072 of 128 x 256 948 and 353.
+// token by token and by chunks: 160 states of 64 x 128 19 and 21 us, 96 sequences of 32 heads of 128 x 256
+// 948 and 353.
 bool delta_recurrent_preferred(int in_dtype, const Dims& d) {
     const double heads = (double)d.batch * d.nheads, million = heads * d.headdim * d.dstate * 1e-6;
     const double chunk = in_dtype == kBF16 ? 18 + 0.008 * heads + 2.5 * million

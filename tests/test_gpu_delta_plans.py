@@ -133,3 +133,46 @@ def test_nan_in_one_head_of_many():
         assert torch.equal(a[n][:, :, [0, 2]], b[n][:, :, [0, 2]]), n
     assert torch.equal(a["dh0"][:, [0, 2]], b["dh0"][:, [0, 2]])
     assert torch.isnan(b["dk"]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 1, 80, 64, 128, 1), (96, 1, 32, 128, 128, 16), (3, 1, 2, 16, 256, 2), (1, 1, 1, 16, 16, 1)])
+def test_step(shape, dtype):
+    # fp32 arithmetic for either type
+    e = _problem(shape, dtype, sum(shape))
+    want_y, want_f, _ = ref.forward(e, 2.0)
+    y = ssd.delta_decode_step(*[e[n][:, 0].contiguous() for n in INPUTS[:5]], e["h0"], scale=2.0)
+    _close(y, want_y[:, 0], TOL["fp32"], "y")
+    _close(e["h0"], want_f, TOL["fp32"], "state")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_layer(dtype):
+    """Delta rule and gated norm of each head's rows, and their gradients, with four waves a workgroup in the
+    walks, two heads a workgroup of the gradients and several turns in the norm. The norm divides y's error by
+    each row's own size, down to a tenth of the usual one; its gradient does so again, and that of the
+    delta rule starts from it."""
+    shape = (130, 65, 6, 64, 32, 1)
+    e = _problem(shape, dtype, 77)
+    b, L, h, P = shape[:4]
+    assert ssd.delta_backward_plan(_shape(e)) == (4, 1, 2)
+    gen = torch.Generator().manual_seed(78)
+    z, w, dout = (dev(torch.randn(s, generator=gen)) for s in ((b, L, h * P), (h * P,), (b, L, h * P)))
+    z = z.to(e["v"].dtype)
+    opts = dict(z=z, groups=h, act="gate_post")
+    y, final = ssd.delta_forward(*[e[n] for n in INPUTS])
+    out = ssd.group_norm(y.flatten(2), w, **opts)
+    back = ssd.group_norm_backward(y.flatten(2), w, None, dout, **opts)
+    grads = ssd.delta_backward(*[e[n] for n in INPUTS], back["dx"].view(b, L, h, P), e["dfinal"])
+    ry, rf, _ = ref.forward(e)
+    leaves = [t.requires_grad_() for t in (ry.flatten(2), w.double(), z.double())]
+    rout = ref.norm(leaves[0], leaves[1], None, leaves[2], h, 1e-5, False, "gate_post")
+    dy, dw, dz = torch.autograd.grad((rout * dout.double()).sum(), leaves)
+    tol = 10 * TOL[dtype]
+    _close(out, rout.detach(), tol, "out")
+    _close(final, rf, TOL[dtype], "final")
+    _close(back["dw"], dw, tol, "dw")
+    _close(back["dz"], dz, tol, "dz")
+    want = ref.backward({**e, "dy": dy.view(b, L, h, P)})
+    for n in want:
+        _close(grads[n], want[n], 10 * tol, n)
